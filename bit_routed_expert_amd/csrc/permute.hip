@@ -298,12 +298,15 @@ unpermute_kernel(int top_k, int P, int K, const void* __restrict__ rows, const i
 
 // d_rows[pos[t, j]] = w[t, j] dy[t], d_w[t, j] = <dy[t], rows[pos[t, j]]>: TOGETHER rows of a token at a time, so
 // that dy is read and the products are summed once for them. The sums are the workgroup's own, in a fixed order.
+// d_rows may be rows: then a thread writes no value that another one's product takes, of the last chunk, moved back
+// to lie in the row, only those that the chunk before does not hold (T = 8192, K = 510: 42 us over rows, 34
+// beside them with the whole chunk written).
 // One workgroup per token, four rows together, and one per pair, top 8, bf16: T = 64 with K = 6144 9.2 and 4.1 us,
 // 512 19.2 and 17.4, 1024 36.2 and 38.9, 8192 320 (1.7 GB, 5.3 TB/s) and 333; K = 512, T = 8192 31 and 49.
 template <class T, int W, int TOGETHER, bool PAST>
 __global__ void __launch_bounds__(kThreads)
-unpermute_backward_kernel(int top_k, int P, int K, const void* __restrict__ dy, const void* __restrict__ rows,
-                          const int32_t* __restrict__ pos, const float* __restrict__ w, void* __restrict__ d_rows,
+unpermute_backward_kernel(int top_k, int P, int K, const void* __restrict__ dy, const void* rows,
+                          const int32_t* __restrict__ pos, const float* __restrict__ w, void* d_rows,
                           float* __restrict__ d_w) {
   __shared__ float part[kThreads / 64][TOGETHER];
   const long long t = blockIdx.x;
@@ -339,8 +342,16 @@ unpermute_backward_kernel(int top_k, int P, int K, const void* __restrict__ dy, 
         float o[W];
 #pragma unroll
         for (int q = 0; q < W; ++q) o[q] = here[i] ? wt[i] * d[q] : 0.f;
-        if constexpr (W == 8) store8<T, PAST>(d_rows, r[i] * K + at, raw8<T>(o));
-        else store1<T>(d_rows, r[i] * K + at, o[0]);
+        if constexpr (W == 8) {
+          if (again == 0 || d_rows != rows) store8<T, PAST>(d_rows, r[i] * K + at, raw8<T>(o));
+          else {
+#pragma unroll
+            for (int q = 1; q < W; ++q)
+              if (q >= again) store1<T>(d_rows, r[i] * K + at + q, o[q]);
+          }
+        } else {
+          store1<T>(d_rows, r[i] * K + at, o[0]);
+        }
         if (!here[i]) continue;
         if constexpr (W == 8) {
           float v[8];

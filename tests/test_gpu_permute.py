@@ -240,3 +240,25 @@ def test_beyond_32_bit_offsets(gpu):
         assert torch.equal(d_rows[at:at + 1000], rows[at:at + 1000])
     sq = x[-100:].double().square().sum(1, keepdim=True) * (pos[-100:] >= 0)
     assert bool(((d_w[-100:].double() - sq).abs() <= K * U * sq).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [513, 517, 519, 1025, 1031, 2050, 4097, 4103])
+@pytest.mark.parametrize("T,top_k", [(61, 3), (520, 5)])
+def test_gradient_over_its_rows_whose_last_chunk_is_another_waves(gpu, T, top_k, K, dtype):
+    """Rows whose last 8 values begin in the last lane of one wave and end in the first of the next, in the same step
+    of both or in neighbouring ones: over rows or not, d_w is the product with rows as they were (multiples of 1/8 of
+    at most 1, so that sums of K products are exact in any order) and d_rows w dy."""
+    rng = np.random.default_rng(K + T)
+    ids = dev(draw_ids(rng, T, top_k, 8))
+    x, dy = [torch.from_numpy(rng.integers(-8, 9, (T, K)) / 8).to(dtype).cuda() for _ in range(2)]
+    rows, _, _, pos = moe.moe_w2_permute(x, ids, 8)
+    w = torch.from_numpy(rng.integers(1, 4, (T, top_k)) * 64.0).float().cuda()      # far from what rows hold
+    here = pos >= 0
+    row = torch.where(here, pos, -1 - pos).long()
+    want_w = torch.where(here, (x.double() * dy.double()).sum(1)[:, None], 0.0).float()
+    want = torch.zeros_like(rows)
+    want[row.flatten()] = (torch.where(here, w, 0.0)[..., None] * dy.float()[:, None]).to(dtype).flatten(0, 1)
+    for d_rows in (None, rows):                                                      # rows last: they are lost
+        got, got_w = moe.moe_w2_unpermute_backward(dy, rows, pos, w, d_rows=d_rows)
+        assert torch.equal(got_w, want_w) and torch.equal(got, want)
