@@ -38,25 +38,18 @@ def quantize(x, fmt):
     x = np.asarray(x, dtype=np.float64)
     R, K = x.shape
     mags = _MAGNITUDES[fmt]
-    codes = np.zeros((R, K), dtype=np.uint8)
-    scales = np.zeros((R, K // 32), dtype=np.uint8)
     limits = mags[-1] * np.ldexp(1.0, np.arange(255) - 127)
     mid = (mags[1:] + mags[:-1]) / 2
-    for r in range(R):
-        for k in range(K // 32):
-            v = x[r, 32 * k:32 * k + 32]
-            if not np.all(np.isfinite(v)):
-                scales[r, k] = 255
-                continue
-            b = int(np.searchsorted(limits, np.abs(v).max()))   # least index with limit >= max
-            scales[r, k] = b
-            t = np.abs(v) / 2.0 ** (b - 127)
-            lo = np.searchsorted(mid, t, side="left")            # midpoints below t
-            tie = np.zeros(32, dtype=bool)
-            inside = lo < len(mid)
-            tie[inside] = t[inside] == mid[lo[inside]]
-            code = lo + (tie & (lo % 2 == 1))                    # between code lo and lo + 1: the even one
-            codes[r, 32 * k:32 * k + 32] = code + np.signbit(v) * (8 if fmt == E2M1 else 128)
+    blocks = x.reshape(R, K // 32, 32)
+    finite = np.isfinite(blocks).all(-1)
+    v = np.where(finite[..., None], blocks, 0.0)
+    b = np.searchsorted(limits, np.abs(v).max(-1))               # least index with limit >= max
+    t = np.abs(v) / np.ldexp(1.0, b - 127)[..., None]
+    lo = np.searchsorted(mid, t, side="left")                    # midpoints below t
+    tie = (lo < len(mid)) & (t == mid[np.minimum(lo, len(mid) - 1)])
+    code = lo + (tie & (lo % 2 == 1)) + np.signbit(v) * (8 if fmt == E2M1 else 128)   # of a tie the even one
+    codes = np.where(finite[..., None], code, 0).astype(np.uint8).reshape(R, K)
+    scales = np.where(finite, b, 255).astype(np.uint8)
     if fmt == E2M1:
         return (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8), scales
     return codes, scales
