@@ -12,7 +12,7 @@ constexpr int kThreads = 256;
 
 // All three kernels are bound by their bytes. Calls whose rows would take more than a quarter of the last cache
 // (256 MB) read and write them past it, which leaves it to the codes and their reader and is faster: norm T = 8192
-// bf16 with K = 4096 48 -> 41 us, K = 6144 70 -> 61 us (5.8 TB/s); 16384 x 4096 values to e2m1 31 -> 28 us
+// bf16 with K = 4096 48 -> 41 us, K = 6144 70 -> 61 us (before its codes were exact over the whole range: 43 and 63); 16384 x 4096 values to e2m1 31 -> 28 us
 // (with four pieces a thread in flight, which small calls are too small for) and back 34 -> 25 us.
 constexpr long long kPastBytes = 64LL << 20;
 
@@ -66,31 +66,28 @@ mx_dequantize_kernel(long long chunks, const uint8_t* __restrict__ codes, const 
   }
 }
 
-// n = (h + low) g (s1 + s2), rounded to nearest, and rounded to odd (its last bit set if it is not exact), whose
-// rounding to fewer bits is n's own. No step may be contracted: the errors are those of the rounded products.
-struct Normed { float near, odd; };
-MOEW2_DEV Normed norm_value(float h, float low, float g, float s1, float s2) {
-#pragma clang fp contract(off)
-  const float p = h * g, e = __builtin_fmaf(low, g, __builtin_fmaf(h, g, -p)), q = p * s1;
-  const float rest = __builtin_fmaf(p, s1, -q) + __builtin_fmaf(p, s2, e * s1), sum = q + rest;
-  const float n = q == 0.f ? q : sum, lost = (q - n) + rest;      // (a zero keeps its sign)
-  const int b = __builtin_bit_cast(int, n);
-  const int step = (lost < 0.f) == (n < 0.f) ? 1 : -1;
-  const bool nudge = (b & 1) == 0 && __builtin_fabsf(n) > 0.f && __builtin_fabsf(lost) > 0.f;   // (not for a NaN)
-  return {n, __builtin_bit_cast(float, nudge ? b + step : b)};
+// v rounded to odd, from its rounding to nearest.
+MOEW2_DEV float to_odd(double v, float near) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, near);
+  const double lost = __builtin_fabs(v) - __builtin_fabs((double)near);      // (NaN: no step; an infinity stays one)
+  const bool step = (b & 1) == 0 && __builtin_isfinite(near);
+  return __builtin_bit_cast(float, b + (step && lost > 0. ? 1u : step && lost < 0. ? ~0u : 0u));
 }
 
-// Bound by the rows' bytes while the arithmetic stays below some 40 instructions a value. That leaves room for codes
-// of the exact n: sums of squares and 1 / rms in double, 1 / rms and the products h gamma as two floats each and, of
-// fp32 rows, what their fp32 sum leaves out (low). An n rounded once to fp32 rounds on to the right element unless it
-// lies on a midpoint of two, whose 19 last bits are 0: then, about once in 2^19 values, the wave takes n rounded to
-// odd (always so: T = 8192, K = 6144 64 us instead of 61, T = 1, K = 4096 4.6 instead of 4.0; without
-// it 59 and 3.5).
+// Bound by the rows' bytes while the arithmetic stays below some 40 instructions a value (all of it in double:
+// T = 8192, K = 6144 81 us instead of 63). That leaves room for codes of the exact n: sums of squares and 1 / rms in
+// double, 1 / rms and the products h gamma as two floats each, of fp32 rows what their fp32 sum leaves out (low). Such
+// an n, rounded once to fp32, rounds on to the right element unless it lies on a midpoint of two, whose 19 last bits
+// are 0, about once in 2^19 values. The wave computes its values in double from x and residual where one lies there,
+// where a sum of two 16-bit values takes more than fp32's 24 bits (they lie 17 binades apart or, in fp16, 14),
+// and where the row leaves the range in which none of the products above overflows or loses bits: h 0 or from 2^-40,
+// gamma from 2^-40 to 2^60, 1 / rms from 2^-20 to 2^30, so that h gamma >= 2^-80 and |n| >= 2^-100 are far above 2^-149.
 // One row per workgroup of NT threads, or, if NT is 64, per wave of a workgroup of four, which needs no barrier:
 // the row stays in registers (CH chunks of 8 values a thread). A wave per row and a workgroup per row, bf16 to e4m3:
 // T = 8192 with K = 128 5.5 and 8.8 us, 512 8.6 and 10.5, 1024 13.0 and 13.9, 2048 24.4 and 22.8; K = 1024 with T = 1
-// 3.6 and 3.0, 1024 4.4 and 4.0, 32768 40 and 53 (all before the codes were made exact, which adds up to 0.8 us). The choice is K's alone, so that the order of a row's sums, and with
-// it every bit of its results, is the same in any batch. T = 1, K = 4096 takes 4.0 us.
+// 3.6 and 3.0, 1024 4.4 and 4.0, 32768 40 and 53 (all before the codes were made exact, which adds 0.3 to 2.5 us). The
+// choice is K's alone, so that the order of a row's sums, and with it every bit of its results, is the same in any
+// batch. bf16 to e4m3, T = 1, K = 4096 takes 4.3 us, T = 32 4.9, T = 8192 43 (5.5 TB/s), K = 6144 63 (5.7 TB/s).
 template <class T, class G, int FMT, int NT, int CH, bool PAST>
 __global__ void __launch_bounds__(NT == 64 ? kThreads : NT)
 add_rmsnorm_mx_kernel(int rows, int K, const void* x, const void* residual, const void* __restrict__ gamma, float eps,
@@ -102,71 +99,123 @@ add_rmsnorm_mx_kernel(int rows, int K, const void* x, const void* residual, cons
   const int chunks = K / 8;
   const long long row = (long long)r * chunks;
   constexpr bool kLow = std::is_same<T, F32>::value;
-  float h[CH][8], low[CH][8];
+  struct Terms { Raw8<T> x, residual; };                      // (no residual: -0, which, added, changes nothing)
+  auto load = [&](int c, Terms& t) {
+    t.x = load8<T, PAST>(x, 8 * (row + c));
+    if (residual) t.residual = load8<T, PAST>(residual, 8 * (row + c));
+    else {
+#pragma unroll
+      for (auto& v : t.residual.v) v = u32x4_t{} + (T::kBytes == 2 ? 0x80008000u : 0x80000000u);
+    }
+  };
+  float h[CH][8], low[kLow ? CH : 1][8], cross = 0.f;
+  bool apart[CH];                                             // a small h, or a sum of two 16-bit values is not exact
   double sum[4] = {0., 0., 0., 0.};
+  Terms terms[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i)                                // all loads together
+    if (tid + i * NT < chunks) load(tid + i * NT, terms[i]);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * NT;
     if (c >= chunks) continue;
-    values8(load8<T, PAST>(x, 8 * (row + c)), h[i]);
-    float v[8] = {-0.f, -0.f, -0.f, -0.f, -0.f, -0.f, -0.f, -0.f};   // (added, it changes nothing)
-    if (residual) values8(load8<T, PAST>(residual, 8 * (row + c)), v);
+    float v[8];
+    values8(terms[i].x, h[i]);
+    values8(terms[i].residual, v);
+    uint32_t wide = 0, small = ~0u;                           // bits that a sum lost; 2 |h| - 1 of the least h but 0
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      double exact;
       if constexpr (kLow) {
-        exact = (double)h[i][j] + (double)v[j];
+        const double exact = (double)h[i][j] + (double)v[j];
         h[i][j] = (float)exact;
         low[i][j] = (float)(exact - (double)h[i][j]);
+        sum[j % 4] = __builtin_fma(exact, exact, sum[j % 4]);
       } else {
-        h[i][j] += v[j];
-        exact = h[i][j];
+        const float both = h[i][j] + v[j], second = both - h[i][j];
+        const float lost = (h[i][j] - (both - second)) + (v[j] - second);
+        h[i][j] = both;
+        wide |= __builtin_bit_cast(uint32_t, lost) << 1;
+        cross = __builtin_fmaf(both, lost, cross);
+        sum[j % 4] = __builtin_fma((double)both, (double)both, sum[j % 4]);
       }
-      sum[j % 4] = __builtin_fma(exact, exact, sum[j % 4]);
+      small = min(small, (__builtin_bit_cast(uint32_t, h[i][j]) << 1) - 1u);
     }
+    apart[i] = wide || small < ((127 - 40) << 24) - 1;
   }
-  double total = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-  if constexpr (!kWave) {
-    __shared__ double part[NT / 64];
-    if ((tid & 63) == 0) part[tid >> 6] = total;
-    __syncthreads();
-    total = 0.;
+  auto over_row = [&](double v, bool first) {
+    v = wave_sum(v);
+    if constexpr (!kWave) {
+      __shared__ double part[NT / 64];
+      if (!first) __syncthreads();
+      if ((tid & 63) == 0) part[tid >> 6] = v;
+      __syncthreads();
+      v = 0.;
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) total += part[w];
+      for (int w = 0; w < NT / 64; ++w) v += part[w];
+    }
+    return 1. / __dsqrt_rn(v / (double)K + (double)eps);
+  };
+  double inv = over_row((sum[0] + sum[1]) + (sum[2] + sum[3]) + 2. * (double)cross, true);
+  const bool extreme = !(inv >= 0x1p-20 && inv <= 0x1p30);    // (the whole row's)
+  if (!kLow && __builtin_expect(extreme, 0)) {
+    double again = 0.;
+    for (int c = tid; c < chunks; c += NT) {
+      float a[8], v[8];
+      Terms t;
+      load(c, t);
+      values8(t.x, a);
+      values8(t.residual, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double exact = (double)a[j] + (double)v[j];
+        again = __builtin_fma(exact, exact, again);
+      }
+    }
+    inv = over_row(again, false);
   }
-  const double inv = 1. / __dsqrt_rn(total / (double)K + (double)eps);
-  const float s1 = (float)inv, s2 = (float)(inv - (double)s1);   // inv = s1 + s2 (s2 NaN with an infinite s1)
+  const float s1 = (float)inv, s2 = (float)(inv - (double)s1);   // inv = s1 + s2
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * NT;
     if (c >= chunks) continue;
-    if (residual_out) store8<T, PAST>(residual_out, 8 * (row + c), raw8<T>(h[i]));
-    float g[8], n[8];
+    float g[8], n[8], odd[8];
     values8(load8<G>(gamma, 8 * c), g);
     uint32_t least = ~0u;
+    float gmin = INFINITY, gmax = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+      gmin = __builtin_fminf(gmin, __builtin_fabsf(g[j]));
+      gmax = __builtin_fmaxf(gmax, __builtin_fabsf(g[j]));
       const float p = h[i][j] * g[j];
       float e = __builtin_fmaf(h[i][j], g[j], -p);
       if constexpr (kLow) e = __builtin_fmaf(low[i][j], g[j], e);
-      n[j] = __builtin_fmaf(p, s1, __builtin_fmaf(p, s2, e * s1));
-      const bool zero = n[j] == 0.f;
-      if (zero) n[j] = p * s1;                     // keeps its sign
-      least = min(least, zero ? 1u : __builtin_bit_cast(uint32_t, n[j]) << 13);
+      n[j] = __builtin_copysignf(__builtin_fmaf(p, s1, __builtin_fmaf(p, s2, e * s1)), p);   // (a zero's sign)
+      least = min(least, __builtin_bit_cast(uint32_t, n[j]) << 13);
+      odd[j] = n[j];
     }
+    bool alone = extreme || apart[i] || !(gmin >= 0x1p-40f && gmax <= 0x1p60f);
     if (__any(least == 0)) {
+      least = 1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) least = min(least, n[j] == 0.f ? 1u : __builtin_bit_cast(uint32_t, n[j]) << 13);
+      alone |= least == 0;
+    }
+    if (__builtin_expect(__any(alone), 0)) {
+      float a[8], v[8];
+      Terms t;
+      load(c, t);
+      values8(t.x, a);
+      values8(t.residual, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const Normed v = norm_value(h[i][j], kLow ? low[i][j] : 0.f, g[j], s1, s2);
-        n[j] = v.near;
-        h[i][j] = v.odd;
+        const double exact = ((double)a[j] + (double)v[j]) * inv * (double)g[j];
+        n[j] = (float)exact;
+        odd[j] = to_odd(exact, n[j]);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = n[j];
     }
+    if (residual_out) store8<T, PAST>(residual_out, 8 * (row + c), raw8<T>(h[i]));
     if (normed) store8<T, PAST>(normed, 8 * (row + c), raw8<T>(n));
-    mx_quantize_chunk<FMT>(h[i], row + c, codes, scales);
+    mx_quantize_chunk<FMT>(odd, row + c, codes, scales);
   }
 }
 

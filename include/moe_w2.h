@@ -445,8 +445,9 @@ int mx_matmul(int M, int N, int K, int a_format, const uint8_t* a_codes, const u
  * add_rmsnorm_mx - the norm in front of the experts, with the residual's addition, into MX codes:
  *   h = x + residual;  n = h / sqrt(mean_k h^2 + eps) * gamma   per row, from the unrounded h
  *   residual_out = h and normed = n, each in fp32 and rounded once to `dtype`; codes, scales =
- * mx_quantize(n) of the unrounded n (held to about 2^-44 of itself, so that elements next to a
- * midpoint round as the exact n's do). x, residual, residual_out, normed [T][K] of `dtype`; gamma [K] of
+ * mx_quantize(n) of the unrounded n (held to about 2^-46 of itself, whatever finite values x,
+ * residual and gamma have, so that elements next to a midpoint round as the exact n's do; an n that
+ * fp32 would round to an infinity is one). eps = 0 makes a row of zeros NaN. x, residual, residual_out, normed [T][K] of `dtype`; gamma [K] of
  * gamma_dtype (`dtype` or MOE_W2_F32). residual may be null (h = x); residual_out and normed may be
  * null (not written). residual_out and normed may be the same memory as x or residual (but not as
  * each other). A row's results are the same in any batch.

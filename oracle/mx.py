@@ -57,7 +57,7 @@ def quantize(x, fmt):
 
 def norm(x, residual, gamma, eps):
     """(h, n) in float64."""
-    h = np.asarray(x, np.float64) + (0.0 if residual is None else np.asarray(residual, np.float64))
+    h = np.asarray(x, np.float64) if residual is None else np.asarray(x, np.float64) + np.asarray(residual, np.float64)
     return h, h / np.sqrt(np.mean(h * h, axis=1, keepdims=True) + eps) * np.asarray(gamma, np.float64)
 
 
