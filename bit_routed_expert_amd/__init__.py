@@ -437,7 +437,7 @@ def _ext():
         try:
             from . import _bind as b
         except ImportError as e:
-            raise ImportError(f"_bind.so is not built; run __graft_entry__.build() ({e})") from e
+            raise ImportError(f"the compiled binding is not built for this Python and PyTorch; run __graft_entry__.build() ({e})") from e
         b.load(LIB_PATH)
         _BIND = b
     return _BIND

@@ -1,6 +1,9 @@
-"""Build libmoew2.so (all HIP sources under csrc/) for gfx950 with hipcc, and _bind.so (csrc/bind.cpp, the
-compiled part of the Python binding, host code) with g++, in-tree."""
+"""Build libmoew2.so (all HIP sources under csrc/) for gfx950 with hipcc, and _bind (csrc/bind.cpp, the
+compiled part of the Python binding, host code, an extension module of this Python and this PyTorch) with
+g++, in-tree. The library needs hipcc alone: it is linked whatever becomes of the binding, which is left
+out where PyTorch is not installed."""
 import concurrent.futures
+import importlib.util
 import os
 import subprocess
 import sys
@@ -9,7 +12,7 @@ import sysconfig
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoew2.so")
-BIND = os.path.join(HERE, "_bind.so")
+BIND = os.path.join(HERE, "_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(HERE, "_build")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -40,7 +43,7 @@ def _build_bind():
     from torch.utils import cpp_extension
     tmp = BIND + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMOEW2_TORCH_VERSION="{torch.__version__}"']
     for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", d]
     cmd += [os.path.join(CSRC, "bind.cpp"), "-o", tmp, "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
@@ -52,24 +55,27 @@ def _build_bind():
     return r.stdout + r.stderr
 
 
-def build(verbose=False):
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        bind = ex.submit(_build_bind)
-        results = list(ex.map(_compile, srcs))
-        results.append((None, bind.result()))
-    if verbose:
-        for obj, out in results:
-            if out.strip():
-                print(out)
-    objs = [o for o, _ in results if o]
+def _link(objs):
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB)
+
+
+def build(verbose=False):
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    srcs = sources()
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        bind = ex.submit(_build_bind) if importlib.util.find_spec("torch") else None
+        results = list(ex.map(_compile, srcs))
+        _link([o for o, _ in results])
+        outs = [out for _, out in results] + ([bind.result()] if bind else ["PyTorch is not installed: no Python binding"])
+    if verbose:
+        for out in outs:
+            if out.strip():
+                print(out)
     return LIB
 
 

@@ -11,6 +11,7 @@
 #include <ATen/ATen.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <string>
 
 #include "../../include/moe_w2.h"
@@ -344,4 +345,14 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind(void) { return PyModule_Create(&module); }
+// Tensors are read through PyTorch's headers, whose layouts go with its version.
+PyMODINIT_FUNC PyInit__bind(void) {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  const char* v = version ? PyUnicode_AsUTF8(version) : nullptr;
+  const bool same = v && !strcmp(v, MOEW2_TORCH_VERSION);
+  if (v && !same) PyErr_Format(PyExc_ImportError, "_bind was built for PyTorch " MOEW2_TORCH_VERSION ", this is %s", v);
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  return same ? PyModule_Create(&module) : nullptr;
+}
