@@ -81,21 +81,44 @@ int dtype_of(at::ScalarType t, const char* name) {
   }
 }
 
-// An output: the caller's, checked, or a new one.
+// An output: the caller's, checked, or one that make() allocates.
 struct Out {
   at::Tensor t;
-  void* p;
+  void* p = nullptr;
+  c10::SmallVector<int64_t, 6> shape;
+  at::ScalarType dtype = at::kByte;
+  int dev = -1;                          // of one to be allocated
+  void make() {
+    if (dev < 0) return;
+    t = at::empty(shape, at::TensorOptions().dtype(dtype).device(at::Device(at::kCUDA, dev)));
+    p = t.data_ptr();
+  }
 };
 Out output(PyObject* o, at::ScalarType dtype, at::IntArrayRef shape, int dev, const char* name) {
   Out r;
   if (o == Py_None) {
-    r.t = at::empty(shape, at::TensorOptions().dtype(dtype).device(at::Device(at::kCUDA, dev)));
-    r.p = r.t.data_ptr();
+    if (dev < 0) raise(PyExc_RuntimeError, "no GPU is in use");
+    r.shape.assign(shape.begin(), shape.end());
+    r.dtype = dtype;
+    r.dev = dev;
   } else {
     r.t = tensor(o, name);
     r.p = address(r.t, dtype, shape, dev, name);
   }
   return r;
+}
+
+// Allocates the outputs and calls the C ABI. Both may wait (for memory, for room in the stream's queue), so
+// other Python threads run meanwhile; once a call, as taking the interpreter back may wait for them.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <class F, class... Outs>
+int call(F&& f, Outs&... outs) {
+  const Unlocked unlocked;
+  (outs.make(), ...);
+  return f();
 }
 
 int integer(PyObject* o) {
@@ -138,9 +161,12 @@ PyObject* quantize(Args a) {   // x, format, codes, scales
   const Rows s = rows_of(x, "x");
   const int dt = dtype_of(x.scalar_type(), "x"), fmt = format_of(a[1]), dev = integer(a[4]);
   const void* px = address(x, x.scalar_type(), x.sizes(), dev, "x");
-  const Out codes = output(a[2], at::kByte, {s.r, code_bytes(s.k, fmt)}, dev, "codes");
-  const Out scales = output(a[3], at::kByte, {s.r, s.k / 32}, dev, "scales");
-  const int st = abi.mx_quantize((int)s.r, (int)s.k, dt, px, fmt, (uint8_t*)codes.p, (uint8_t*)scales.p, handle(a[5]));
+  Out codes = output(a[2], at::kByte, {s.r, code_bytes(s.k, fmt)}, dev, "codes");
+  Out scales = output(a[3], at::kByte, {s.r, s.k / 32}, dev, "scales");
+  void* const stream = handle(a[5]);
+  const int st = call([&] {
+    return abi.mx_quantize((int)s.r, (int)s.k, dt, px, fmt, (uint8_t*)codes.p, (uint8_t*)scales.p, stream);
+  }, codes, scales);
   return st ? status(st) : give(codes.t, scales.t);
 }
 
@@ -151,9 +177,12 @@ PyObject* dequantize(Args a) {   // codes, scales, format, dtype (enum moe_w2_dt
   const int64_t k = fmt == MOE_MX_E2M1 ? 2 * s.k : s.k;
   const void* pc = address(codes, at::kByte, codes.sizes(), dev, "codes");
   const void* ps = address(a[1], at::kByte, {s.r, k / 32}, dev, "scales");
-  const Out x = output(a[4], dt == MOE_W2_F32 ? at::kFloat : dt == MOE_W2_F16 ? at::kHalf : at::kBFloat16, {s.r, k}, dev, "x");
+  Out x = output(a[4], dt == MOE_W2_F32 ? at::kFloat : dt == MOE_W2_F16 ? at::kHalf : at::kBFloat16, {s.r, k}, dev, "x");
   if (k > INT32_MAX) raise(PyExc_ValueError, "codes has too long rows");
-  const int st = abi.mx_dequantize((int)s.r, (int)k, fmt, (const uint8_t*)pc, (const uint8_t*)ps, dt, x.p, handle(a[6]));
+  void* const stream = handle(a[6]);
+  const int st = call([&] {
+    return abi.mx_dequantize((int)s.r, (int)k, fmt, (const uint8_t*)pc, (const uint8_t*)ps, dt, x.p, stream);
+  }, x);
   return st ? status(st) : give(x.t);
 }
 
@@ -169,9 +198,12 @@ PyObject* matmul(Args a) {   // a_codes, a_scales, w_codes, w_scales, a_format, 
   const void* psa = address(a[1], at::kByte, {s.r, k / 32}, dev, "a_scales");
   const void* pw = address(wc, at::kByte, {n, k / 2}, dev, "w_codes");
   const void* psw = address(a[3], at::kByte, {n, k / 32}, dev, "w_scales");
-  const Out y = output(a[6], out == MOE_W2_OUT_F32 ? at::kFloat : at::kBFloat16, {s.r, n}, dev, "y");
-  const int st = abi.mx_matmul((int)s.r, (int)n, (int)k, fmt, (const uint8_t*)pa, (const uint8_t*)psa, (const uint8_t*)pw,
-                               (const uint8_t*)psw, y.p, out, handle(a[8]));
+  Out y = output(a[6], out == MOE_W2_OUT_F32 ? at::kFloat : at::kBFloat16, {s.r, n}, dev, "y");
+  void* const stream = handle(a[8]);
+  const int st = call([&] {
+    return abi.mx_matmul((int)s.r, (int)n, (int)k, fmt, (const uint8_t*)pa, (const uint8_t*)psa, (const uint8_t*)pw,
+                         (const uint8_t*)psw, y.p, out, stream);
+  }, y);
   return st ? status(st) : give(y.t);
 }
 
@@ -186,14 +218,16 @@ PyObject* add_rmsnorm(Args a) {   // x, residual, gamma, eps, format, normed (te
   const void* px = address(x, t, x.sizes(), dev, "x");
   const void* pr = a[1] == Py_None ? nullptr : address(a[1], t, x.sizes(), dev, "residual");
   const void* pg = address(gamma, gamma.scalar_type(), {s.k}, dev, "gamma");
-  const Out h = output(a[6], t, x.sizes(), dev, "residual_out");
+  Out h = output(a[6], t, x.sizes(), dev, "residual_out");
   Out n;
-  n.p = nullptr;
   if (a[5] != Py_None) n = output(a[5] == Py_True ? Py_None : a[5], t, x.sizes(), dev, "normed");
-  const Out codes = output(a[7], at::kByte, {s.r, code_bytes(s.k, fmt)}, dev, "codes");
-  const Out scales = output(a[8], at::kByte, {s.r, s.k / 32}, dev, "scales");
-  const int st = abi.add_rmsnorm_mx((int)s.r, (int)s.k, dt, px, pr, pg, gdt, (float)eps, h.p, n.p, fmt, (uint8_t*)codes.p,
-                                    (uint8_t*)scales.p, handle(a[10]));
+  Out codes = output(a[7], at::kByte, {s.r, code_bytes(s.k, fmt)}, dev, "codes");
+  Out scales = output(a[8], at::kByte, {s.r, s.k / 32}, dev, "scales");
+  void* const stream = handle(a[10]);
+  const int st = call([&] {
+    return abi.add_rmsnorm_mx((int)s.r, (int)s.k, dt, px, pr, pg, gdt, (float)eps, h.p, n.p, fmt, (uint8_t*)codes.p,
+                              (uint8_t*)scales.p, stream);
+  }, h, n, codes, scales);
   return st ? status(st) : give(codes.t, scales.t, h.t, n.t);
 }
 
@@ -211,20 +245,22 @@ PyObject* permute(Args a) {   // x, topk_ids, E, rows, workspace
   if (s.k < 1 || P > (1LL << 30)) return status(s.k < 1 ? MOE_W2_EINVAL : MOE_W2_EUNSUPPORTED);
   c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
   shape[0] = P;
-  const Out rows = output(a[3], x.scalar_type(), shape, dev, "rows");
+  Out rows = output(a[3], x.scalar_type(), shape, dev, "rows");
   Out w;
-  w.p = nullptr;
   if (a[4] != Py_None) {
     w.t = tensor(a[4], "workspace");
     w.p = address(w.t, at::kByte, w.t.sizes(), dev, "workspace");
   } else if (P > MOE_W2_PERMUTE_SMALL_PAIRS) {
     w = output(Py_None, at::kByte, {(int64_t)abi.moe_w2_permute_workspace_bytes(E, (int)s.r, (int)s.k)}, dev, "workspace");
   }
-  const Out offsets = output(Py_None, at::kInt, {E < 0 ? 0 : E + 1LL}, dev, "offsets");
-  const Out perm = output(Py_None, at::kInt, {P}, dev, "perm");
-  const Out pos = output(Py_None, at::kInt, {s.r, s.k}, dev, "pos");
-  const int st = abi.moe_w2_permute(E, (int)s.r, (int)s.k, (const int32_t*)pi, px, row_bytes, rows.p, (int32_t*)offsets.p,
-                                    (int32_t*)perm.p, (int32_t*)pos.p, w.p, w.p ? (size_t)w.t.numel() : 0, handle(a[6]));
+  Out offsets = output(Py_None, at::kInt, {E < 0 ? 0 : E + 1LL}, dev, "offsets");
+  Out perm = output(Py_None, at::kInt, {P}, dev, "perm");
+  Out pos = output(Py_None, at::kInt, {s.r, s.k}, dev, "pos");
+  void* const stream = handle(a[6]);
+  const int st = call([&] {
+    return abi.moe_w2_permute(E, (int)s.r, (int)s.k, (const int32_t*)pi, px, row_bytes, rows.p, (int32_t*)offsets.p,
+                              (int32_t*)perm.p, (int32_t*)pos.p, w.p, w.p ? (size_t)w.t.numel() : 0, stream);
+  }, rows, w, offsets, perm, pos);
   return st ? status(st) : give(rows.t, offsets.t, perm.t, pos.t);
 }
 
@@ -254,16 +290,20 @@ Pairs pairs_of(PyObject* rows, const char* name, PyObject* pos, PyObject* w, int
 PyObject* unpermute(Args a) {   // rows, pos, topk_w, y
   const int dev = integer(a[4]);
   const Pairs p = pairs_of(a[0], "rows", a[1], a[2], dev);
-  const Out y = output(a[3], p.t, {p.T, p.K}, dev, "y");
-  const int st = abi.moe_w2_unpermute(p.T, p.top_k, p.K, p.dtype, p.rows, p.pos, (const float*)p.w, y.p, handle(a[5]));
+  Out y = output(a[3], p.t, {p.T, p.K}, dev, "y");
+  void* const stream = handle(a[5]);
+  const int st = call([&] {
+    return abi.moe_w2_unpermute(p.T, p.top_k, p.K, p.dtype, p.rows, p.pos, (const float*)p.w, y.p, stream);
+  }, y);
   return st ? status(st) : give(y.t);
 }
 
 PyObject* permute_backward(Args a) {   // d_rows, pos, dx
   const int dev = integer(a[3]);
   const Pairs p = pairs_of(a[0], "d_rows", a[1], nullptr, dev);
-  const Out dx = output(a[2], p.t, {p.T, p.K}, dev, "dx");
-  const int st = abi.moe_w2_permute_backward(p.T, p.top_k, p.K, p.dtype, p.rows, p.pos, dx.p, handle(a[4]));
+  Out dx = output(a[2], p.t, {p.T, p.K}, dev, "dx");
+  void* const stream = handle(a[4]);
+  const int st = call([&] { return abi.moe_w2_permute_backward(p.T, p.top_k, p.K, p.dtype, p.rows, p.pos, dx.p, stream); }, dx);
   return st ? status(st) : give(dx.t);
 }
 
@@ -271,10 +311,13 @@ PyObject* unpermute_backward(Args a) {   // dy, rows, pos, topk_w, d_rows, d_w
   const int dev = integer(a[6]);
   const Pairs p = pairs_of(a[1], "rows", a[2], a[3], dev);
   const void* dy = address(a[0], p.t, {p.T, p.K}, dev, "dy");
-  const Out d_rows = output(a[4], p.t, {(int64_t)p.T * p.top_k, p.K}, dev, "d_rows");
-  const Out d_w = output(a[5], at::kFloat, {p.T, p.top_k}, dev, "d_w");
-  const int st = abi.moe_w2_unpermute_backward(p.T, p.top_k, p.K, p.dtype, dy, p.rows, p.pos, (const float*)p.w, d_rows.p,
-                                               (float*)d_w.p, handle(a[7]));
+  Out d_rows = output(a[4], p.t, {(int64_t)p.T * p.top_k, p.K}, dev, "d_rows");
+  Out d_w = output(a[5], at::kFloat, {p.T, p.top_k}, dev, "d_w");
+  void* const stream = handle(a[7]);
+  const int st = call([&] {
+    return abi.moe_w2_unpermute_backward(p.T, p.top_k, p.K, p.dtype, dy, p.rows, p.pos, (const float*)p.w, d_rows.p,
+                                         (float*)d_w.p, stream);
+  }, d_rows, d_w);
   return st ? status(st) : give(d_rows.t, d_w.t);
 }
 
