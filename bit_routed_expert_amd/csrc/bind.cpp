@@ -242,7 +242,8 @@ PyObject* permute(Args a) {   // x, topk_ids, E, rows, workspace
   const int64_t P = s.r * s.k;
   const void* px = address(x, x.scalar_type(), x.sizes(), dev, "x");
   const void* pi = address(ids, at::kInt, ids.sizes(), dev, "topk_ids");
-  if (s.k < 1 || P > (1LL << 30)) return status(s.k < 1 ? MOE_W2_EINVAL : MOE_W2_EUNSUPPORTED);
+  const size_t need = abi.moe_w2_permute_workspace_bytes(E, (int)s.r, (int)s.k);
+  if (!need) return status(E < 1 || s.k < 1 ? MOE_W2_EINVAL : MOE_W2_EUNSUPPORTED);   // before outputs of such sizes
   c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
   shape[0] = P;
   Out rows = output(a[3], x.scalar_type(), shape, dev, "rows");
@@ -251,9 +252,9 @@ PyObject* permute(Args a) {   // x, topk_ids, E, rows, workspace
     w.t = tensor(a[4], "workspace");
     w.p = address(w.t, at::kByte, w.t.sizes(), dev, "workspace");
   } else if (P > MOE_W2_PERMUTE_SMALL_PAIRS) {
-    w = output(Py_None, at::kByte, {(int64_t)abi.moe_w2_permute_workspace_bytes(E, (int)s.r, (int)s.k)}, dev, "workspace");
+    w = output(Py_None, at::kByte, {(int64_t)need}, dev, "workspace");
   }
-  Out offsets = output(Py_None, at::kInt, {E < 0 ? 0 : E + 1LL}, dev, "offsets");
+  Out offsets = output(Py_None, at::kInt, {E + 1LL}, dev, "offsets");
   Out perm = output(Py_None, at::kInt, {P}, dev, "perm");
   Out pos = output(Py_None, at::kInt, {s.r, s.k}, dev, "pos");
   void* const stream = handle(a[6]);

@@ -18,7 +18,8 @@ NAMES = ["mx_quantize", "mx_dequantize", "mx_matmul", "add_rmsnorm_mx", "moe_w2_
 def waiting(gpu, tmp_path):
     """The binding on a library whose calls wait 0.2 s on the host and do nothing."""
     src = tmp_path / "waiting.cpp"
-    src.write_text("#include <unistd.h>\n" + "".join(f'extern "C" long {n}() {{ usleep(200000); return 0; }}\n' for n in NAMES))
+    body = {n: "usleep(200000); return 0;" for n in NAMES} | {"moe_w2_permute_workspace_bytes": "return 64;"}
+    src.write_text("#include <unistd.h>\n" + "".join(f'extern "C" long {n}() {{ {b} }}\n' for n, b in body.items()))
     subprocess.run(["g++", "-shared", "-fPIC", str(src), "-o", str(tmp_path / "waiting.so")], check=True, timeout=100)
     torch.zeros(1, device="cuda")
     moe._ext().load(str(tmp_path / "waiting.so"))
@@ -53,3 +54,17 @@ def test_other_threads_run_while_a_call_waits(waiting):
     finally:
         stop.set()
         thread.join()
+
+
+def test_permute_refuses_sizes_before_it_allocates(gpu):
+    x = torch.zeros((40, 2048), device="cuda")
+    ids = torch.zeros((40, 33), dtype=torch.int32, device="cuda")
+    before = torch.cuda.memory_allocated()
+    for n, top_k, E, status in ((40, 8, 2**31 - 1, -2), (40, 8, 1025, -2), (40, 33, 8, -2), (40, 8, 0, -1), (40, 8, -1, -1)):
+        torch.cuda.reset_peak_memory_stats()
+        i = ids[:n, :top_k].contiguous()
+        with pytest.raises(moe.MoeW2Error) as e:
+            moe.moe_w2_permute(x, i, E)
+        assert e.value.status == status
+        assert torch.cuda.max_memory_allocated() - before < 1 << 20      # rows alone would take 2.6 MB
+        del i
