@@ -423,7 +423,8 @@ def moe_w2_codebook_sweep(x, codebooks):
 # ------------------------------------------------------------------------------------------------
 # Operators around the experts. Their marshalling is compiled (csrc/bind.cpp): tensors are checked for type,
 # shape, contiguity and device, outputs that are not given are allocated on the current device, and the C ABI
-# is called on its current stream.
+# is called on its current stream. Outputs carry no autograd history, whatever the inputs require; the gradients are
+# calls of their own.
 # ------------------------------------------------------------------------------------------------
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}   # enum moe_w2_dtype
 PERMUTE_SMALL_PAIRS = 4096                                           # MOE_W2_PERMUTE_SMALL_PAIRS
@@ -472,7 +473,7 @@ def mx_dequantize(codes, scales, format, dtype=torch.bfloat16, x=None):
 
 def mx_matmul(a_codes, a_scales, w_codes, w_scales, a_format=MX_E2M1, out_dtype=OUT_BF16, y=None):
     """y [M, N] = A W^T: A [M, K] in MX of either format, W [N, K] in MXFP4 (w_codes [N, K/2],
-    w_scales [N, K/32] uint8); y bfloat16 (OUT_BF16) or float32 (OUT_F32)."""
+    w_scales [N, K/32] uint8); y float32 (OUT_F32), summed in fp32, or that rounded once to bfloat16 (OUT_BF16)."""
     return _done(_ext().mx_matmul(a_codes, a_scales, w_codes, w_scales, a_format, out_dtype, y, *_where()), "mx_matmul")
 
 
@@ -480,7 +481,7 @@ def add_rmsnorm_mx(x, residual, gamma, eps, format=MX_E4M3, normed=False, residu
     """h = x + residual (residual may be None), n = h / sqrt(mean h^2 + eps) * gamma per row of x [T, K].
     Returns (codes, scales, residual_out, normed): n in MX, h and n in x's type (normed: True, a tensor to
     write, or False, which returns None). gamma [K] of x's type or float32. residual_out and normed may be x
-    or residual themselves."""
+    or residual themselves. It has no gradient call: detach what requires gradients, or use torch's operations there."""
     return _done(_ext().add_rmsnorm_mx(x, residual, gamma, eps, format, None if normed is False else normed, residual_out,
                                         codes, scales, *_where()), "add_rmsnorm_mx")
 
@@ -492,19 +493,19 @@ def moe_w2_permute_workspace_bytes(E, T, top_k):
 def moe_w2_permute(x, topk_ids, E, rows=None, workspace=None):
     """x [T, ...] rows of any type, topk_ids [T, top_k] int32 -> (rows [T*top_k, ...]: token perm[r] // top_k's
     row in expert order, zeros for pairs of no expert; offsets [E+1], perm [T*top_k] as moe_w2_route; pos
-    [T, top_k] int32: a pair's row, or -1 - row for a pair of no expert)."""
+    [T, top_k] int32: a pair's row, or -1 - row for a pair of no expert). Its gradient: moe_w2_permute_backward."""
     return _done(_ext().moe_w2_permute(x, topk_ids, E, rows, workspace, *_where()), "moe_w2_permute")
 
 
 def moe_w2_unpermute(rows, pos, topk_w, y=None):
     """rows [T*top_k, K], pos [T, top_k] (of moe_w2_permute), topk_w [T, top_k] float32 or None for ones ->
-    y [T, K] of rows' type: y[t] = sum_j topk_w[t, j] rows[pos[t, j]]."""
+    y [T, K] of rows' type: y[t] = sum_j topk_w[t, j] rows[pos[t, j]]. Its gradients: moe_w2_unpermute_backward."""
     return _done(_ext().moe_w2_unpermute(rows, pos, topk_w, y, *_where()), "moe_w2_unpermute")
 
 
 def moe_w2_unpermute_backward(dy, rows, pos, topk_w, d_rows=None, d_w=None):
     """Gradients of moe_w2_unpermute(rows, pos, topk_w) for dy [T, K]: (d_rows [T*top_k, K] of rows' type, zero
-    for pairs of no expert; d_w [T, top_k] float32)."""
+    for pairs of no expert; d_w [T, top_k] float32). d_rows may be rows themselves."""
     return _done(_ext().moe_w2_unpermute_backward(dy, rows, pos, topk_w, d_rows, d_w, *_where()), "moe_w2_unpermute_backward")
 
 

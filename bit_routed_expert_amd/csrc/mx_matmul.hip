@@ -23,7 +23,7 @@ typedef uint32_t u32x2u_t __attribute__((vector_size(8), aligned(1)));    // 8 b
 // of 2^-1 below 2^9, those of field 0 .. 8 multiples of 2^-9 below 4, so products with e2m1 (multiples of 1/2,
 // largest power 4) keep every bit: 2^-2 = 2^(8 + 2 - 12) and 2^-10 = 2^(1 + 2 - 13). A bf16 result needs that
 // too: the elements as they are would leave it off by up to 7 * 2^-13 of the terms' magnitudes where large
-// products cancel, and round 1 in some 300 ordinary values to the other neighbour.
+// products cancel, and round one in 240 of a product of normal rows (K = 4096) to the other neighbour.
 template <int FMT>
 MOEW2_DEV f32x4_t mx_mfma_as(const i32x8_t& w, const i32x8_t& a, f32x4_t c, uint32_t sw, uint32_t sa) {
   const f32x4e_t r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
@@ -648,12 +648,12 @@ mx_matmul_split_kernel(int M, int N, int K, const uint8_t* __restrict__ a_codes,
 // A step is 64 reduction elements: 2 groups of a fragment of A with the 4 of W. The reads of a step's
 // operands go out in the step before, across stages too: the barrier that hands over a stage sits before
 // its last step, when this stage's last reads are done, and the loads of the stage after next follow it.
-// M = 8192, N = K = 4096, operands in the last cache: 79 - 85 us with e2m1 rows (3.3 PFLOP/s), 184 - 187 with e4m3,
-// whose products take four times the matrix cycles (half the rate, two operands). e2m1 rows are bound by the loads' way to LDS, which only two stages of 64 KB fit: without the products 66 us are left,
-// without the operands' reads too 64.
-// Every 4096 more of K takes 72 us, with all rows in the XCD's L2 55. (Asking for later stages' rows early, so that
-// they are there, wins 3 to 7% at K = 8192 and loses as much at 4096; four stages of half the length take half
-// lines and won nothing.)
+// M = 8192, N = K = 4096, operands in the last cache: 79 - 85 us with e2m1 rows (3.3 PFLOP/s), 184 - 187 with e4m3;
+// from memory 90 - 104 and 204 - 253. e4m3 rows take four times the matrix cycles (half the rate, two operands): 109 us
+// of the 184. e2m1 rows are bound by the loads' way to LDS, which only two stages of 64 KB fit: without the products
+// 66 us are left, without the operands' reads too 64. Every 4096 more of K takes 72 us, with all rows in the XCD's L2
+// 55. (Asking for later stages' rows early, so that they are there, wins 3 to 7% at K = 8192 and loses as much at
+// 4096; four stages of half the length take half lines and won nothing.)
 // ------------------------------------------------------------------------------------------
 typedef float f32x16a_t __attribute__((ext_vector_type(16)));
 

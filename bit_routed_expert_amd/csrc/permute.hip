@@ -13,7 +13,7 @@ constexpr int kThreads = 256;
 MOEW2_DEV int bin_of(int id, int E) { return (id >= 0 && id < E) ? id : E; }
 
 // Rows beyond the 256 MB that the chip's last cache holds are read and written past it: a reader would find only the
-// last ones there, and the passes themselves are faster (805 MB of rows, with and without: the copy 171 and 193 us,
+// last ones there, and the passes themselves are faster (805 MB of rows, with and without, its other operands in that cache: the copy 171 and 193 us,
 // the weighted sum 162 and 182, the gradient 318 and 347; rows that fit are read up to 15% slower that way).
 constexpr long long kCacheBytes = 256LL << 20;
 
@@ -137,7 +137,8 @@ permute_small_kernel(int E, int T, int top_k, const int32_t* __restrict__ ids, c
 
 // More pairs, in three launches: ranks and counts of chunks of kChunk pairs, sums of the counts over the chunks
 // before, and the copy, whose workgroups add the three parts of a row's index: first row of its expert, pairs of
-// the expert in earlier chunks, rank in its chunk. T = 8192, top 8, K = 6144: 162 us for 906 MB (5.6 TB/s).
+// the expert in earlier chunks, rank in its chunk. T = 8192, top 8, K = 6144: 162 us
+// for 906 MB (5.6 TB/s) with x in the last cache; from memory the copy alone takes 181 - 192, the ranks 10.
 constexpr int kChunk = kThreads;
 
 // The lanes of a pair's expert in its wave come from one ballot per bit of the expert; ranks across the waves from

@@ -433,7 +433,8 @@ int mx_dequantize(int R, int K, int format, const uint8_t* codes, const uint8_t*
  * mx_matmul - y [M][N] = sum_k A[m,k] W[n,k]: the product of MX activations A [M][K] (either
  * format) with an MXFP4 matrix W [N][K] on the block-scaled matrix instruction, e.g. a shared
  * expert's or a projection's. Products are exact, sums are held in fp32, y is fp32
- * (MOE_W2_OUT_F32) or that rounded once to nearest even (MOE_W2_OUT_BF16). A scale byte 255 or an
+ * (MOE_W2_OUT_F32) or that rounded once to nearest even (MOE_W2_OUT_BF16). Results below fp32's
+ * normal range (2^-126) may come out as any value up to it, 0 among them. A scale byte 255 or an
  * e4m3 NaN makes its row of A (its column of y for W) NaN.
  *   M, N >= 0, K > 0 a multiple of 32 (MOE_W2_EUNSUPPORTED otherwise), M, N <= 2^24, K <= 2^23.
  *   y must be 16-byte aligned.
