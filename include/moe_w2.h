@@ -408,7 +408,8 @@ int moe_w2_codebook_sweep(int n, int R, int C, const float* x, int M, const floa
  *   MOE_MX_E4M3 (MXFP8)  codes [R][K], one OCP E4M3FN byte per element
  *   scales [R][K/32]
  * Rows are contiguous and adjacent. Unless said otherwise pointers to elements (of any type) and
- * codes must be 16-byte aligned (MOE_W2_EINVAL otherwise); scale bytes may lie anywhere. These calls
+ * codes must be 16-byte aligned (MOE_W2_EINVAL otherwise); scale bytes may lie anywhere. Outputs may
+ * not overlap each other or inputs, unless said otherwise. These calls
  * are asynchronous, allocate nothing and can be captured; repeated calls are bit-identical.
  */
 enum moe_w2_dtype { MOE_W2_BF16 = 0, MOE_W2_F32 = 1, MOE_W2_F16 = 2 };
